@@ -142,12 +142,14 @@ __device__ __forceinline__ uint32_t mag_max8(const float x[8]) {
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
   return m;
 }
-// max |x| over the values that are no NaN (the comparisons drop one; the sign is
-// dropped for free, unlike in integers).
-__device__ __forceinline__ float finite_max8(const float x[8]) {
-  float m = __builtin_fabsf(x[0]);
+// max |x| over the values that are no NaN, 0 if none (the maximum of a number and a
+// NaN is the number, so it starts from one; the sign is dropped for free, unlike in
+// integers). A signalling NaN, which only memory can hold, is made quiet first: the
+// instruction would return it. On values that were computed that costs nothing.
+__device__ __forceinline__ float number_max8(const float x[8]) {
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(x[i]));
+  for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(__builtin_canonicalizef(x[i])));
   return m;
 }
 // The same of the values as bf16 stores them.
@@ -217,7 +219,7 @@ struct Mx8In {
 template <bool NT = false>
 __device__ __forceinline__ uint32_t mx8_store(const Mx8Out& q, int64_t r, uint32_t c, uint32_t n, const float x[8],
                                               uint32_t& block_mag) {
-  block_mag = quad_max(__float_as_uint(finite_max8(x)));
+  block_mag = quad_max(__float_as_uint(number_max8(x)));
   const uint32_t byte = mx8_byte(block_mag);
   const uint2 w = mx8_pack8(x, mx8_factor(byte));
   if ((c & ~31u) < n) {

@@ -1,0 +1,105 @@
+"""NaN, infinities and padding in the operators around the FP4 product: what
+one bad value may reach, and what it may not."""
+import numpy as np
+import pytest
+
+import layer_ref as ref
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fp4():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import fp4_fully_quantized_amd as m
+    m.lib()
+    return m
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def equal_codes(got, want):
+    """The same codes, a NaN of either sign being one."""
+    assert np.array_equal(np.where(want == 127, got & 127, got), want)
+
+
+def check_mx8(q, x, what):
+    """q is the 8-bit form of x (float64, finite or NaN) by the definition."""
+    codes, scales = ref.mx8_encode(x)
+    assert np.array_equal(q.scales.cpu().numpy(), scales), what
+    equal_codes(q.codes.cpu().numpy(), codes)
+
+
+# ---------------------------------------------------------------- 8 bits
+# Runs of NaN in a row of 96 (first column, length): inside a lane's eight columns, just those, across them, a
+# whole block, a block and more, the end of the row.
+RUNS = [(5, 1), (8, 7), (8, 8), (4, 8), (16, 16), (32, 32), (24, 48), (88, 8), (64, 32), (0, 96)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [96, 91])
+def test_mx8_runs_of_nan_leave_their_block(fp4, kind, cols):
+    """A NaN is E4M3's NaN and does not count for its block's maximum, however many of them there are, quiet or
+    signalling."""
+    import torch
+    say("mx8 runs of NaN", kind, cols)
+    x = np.random.default_rng(8).standard_normal((2 * len(RUNS), 96)).astype(np.float32) * 3
+    t = torch.from_numpy(x).to({"bf16": torch.bfloat16, "f32": torch.float32}[kind])
+    bits = t.view(torch.int16 if kind == "bf16" else torch.int32)
+    for i, (at, n) in enumerate(RUNS):
+        for row, quiet in ((2 * i, True), (2 * i + 1, False)):
+            bits[row, at:at + n] = (0x7FC0 if quiet else 0x7F81) << (0 if kind == "bf16" else 16)
+    t = t.to("cuda")[:, :cols]
+    want = host(t)
+    assert np.isnan(want).any()
+    q = fp4.mx8_quantize(t)
+    check_mx8(q, want, "mx8")
+    back = host(fp4.mx8_dequantize(q))
+    assert np.array_equal(np.isnan(back), np.isnan(want))
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("mnk", [(5, 96, 256), (300, 1096, 512), (4096, 4160, 256)])
+def test_gemm_fused_checkpoint_of_nan(fp4, mnk, fmt):
+    """Bias columns of NaN (a lane's eight, and a whole block): z is NaN there, the rest of each block is z's own
+    8-bit form; few-tile kernel, tile edges and whole tiles."""
+    import torch
+    say("gemm fused z8 of NaN", mnk, fmt)
+    M, N, K = mnk
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    A = fp4.quantize(torch.randn((M, K), generator=gen, device="cuda"), fmt=fmt)
+    B = fp4.quantize(torch.randn((N, K), generator=gen, device="cuda") * 0.05, fmt=fmt)
+    b = torch.randn(N, generator=gen, device="cuda")
+    clean, q0 = fp4.gemm_fused(A, B, bias=b, checkpoint=True)
+    bad = torch.zeros(N, dtype=torch.bool, device="cuda")
+    bad[8:16] = bad[32:64] = bad[N - 32:N - 24] = True
+    b[bad] = float("nan")
+    y, q = fp4.gemm_fused(A, B, bias=b, checkpoint=True)
+    assert torch.equal(torch.isnan(y), bad.expand(M, N)) and torch.equal(y[:, ~bad], clean[:, ~bad])
+    rows = slice(0, M, max(1, M // 40))   # the definition on the host, on some of the rows
+    codes, scales = ref.mx8_encode(host(y[rows]))
+    assert np.array_equal(q.scales[rows].cpu().numpy(), scales)
+    equal_codes(q.codes[rows].cpu().numpy(), codes)
+    whole = fp4.mx8_quantize(y)
+    assert torch.equal(q.codes, whole.codes) and torch.equal(q.scales, whole.scales)
+
+
+@pytest.mark.parametrize("cols", [300, 5000, 20000])
+def test_norm_checkpoint_of_nan(fp4, cols):
+    """A residual row with a run of NaN: h8 is h's 8-bit form."""
+    import torch
+    say("norm h8 of NaN", cols)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    x = torch.randn((6, cols), generator=gen, device="cuda")
+    r = torch.randn((6, cols), generator=gen, device="cuda")
+    r[2, 40:48] = float("nan")
+    r[4, 64:96] = float("nan")
+    o = fp4.rmsnorm(x, torch.ones(cols, device="cuda"), residual=r, h8=True)
+    check_mx8(o.h8, host(x + r), "h8")
+    assert np.array_equal(np.isnan(host(fp4.mx8_dequantize(o.h8))), np.isnan(host(x + r)))
