@@ -255,8 +255,9 @@ def _check_scalar(t, name: str, dtype, count: int, device):
     del torch
 
 
-def _check_qtensor(q, name: str, device=None):
-    """The QTensor's buffers exist on the device and hold rows x cols codes and scales."""
+def _check_qtensor(q, name: str, device=None, amax: bool = False):
+    """The QTensor's buffers exist on the device and hold rows x cols codes and
+    scales; amax: the call needs the tensor amax too (NVFP4)."""
     import torch
     if not isinstance(q, QTensor):
         raise TypeError(f"{name} must be a QTensor")
@@ -269,7 +270,8 @@ def _check_qtensor(q, name: str, device=None):
         if need == 0 or t.numel() < need:
             raise ValueError(f"{name}.{part} holds {t.numel()} bytes, {q.rows} x {q.cols} needs {need}")
     if q.fmt == FP4_NVFP4:
-        _check_scalar(q.amax, f"{name}.amax", torch.float32, 1, device)
+        if amax or q.amax is not None:
+            _check_scalar(q.amax, f"{name}.amax", torch.float32, 1, device)
         _check_scalar(q.tscale, f"{name}.tscale", torch.float32, 1, device)
 
 
@@ -280,7 +282,14 @@ def _check_quant_out(src, out, axis: int, name: str = "out"):
     if (out.rows, out.cols) != want:
         raise ValueError(f"{name} is {out.rows} x {out.cols}; quantizing a {R} x {C} source along "
                          f"{'rows' if axis == FP4_AXIS_ROWS else 'cols'} needs {want[0]} x {want[1]}")
-    _check_qtensor(out, name, src.device)
+    _check_qtensor(out, name, src.device, amax=True)
+
+
+def _amax_of(x):
+    """The tensor amax of amax_from: of a QTensor, or of a result that has one."""
+    if getattr(x, "amax", None) is None:
+        raise ValueError("amax_from has no amax")
+    return x.amax
 
 
 # ---------------------------------------------------------------- tensors
@@ -308,14 +317,14 @@ class QTensor:
     def wrap(cls, codes, scales, fmt: int, amax=None, tscale=None, had_signs: int | None = None) -> "QTensor":
         """A QTensor on tensors the caller has (a loaded weight, a slice of
         whole rows): codes uint8 [rows, cols / 2], scales uint8 [rows, cols / B],
-        both contiguous; NVFP4 needs tscale, and amax where a call takes it
-        (the tensor scale's own tensor stands in for it otherwise). Checked by
-        the calls that take it."""
+        both contiguous; NVFP4 needs tscale. Products and dequantizations need
+        no amax; without one the tensor serves neither as a quantization's
+        output nor as amax_from. Checked by the calls that take it."""
         q = cls.__new__(cls)
         q.rows, q.cols, q.fmt = codes.shape[0], 2 * codes.shape[1], fmt
         q.codes, q.scales = codes, scales
         q.tscale = tscale if fmt == FP4_NVFP4 else None
-        q.amax = (amax if amax is not None else tscale) if fmt == FP4_NVFP4 else None
+        q.amax = amax if fmt == FP4_NVFP4 else None
         q.had_on = had_signs is not None
         q.had_signs = int(had_signs or 0)
         return q
@@ -486,7 +495,7 @@ def quantize_2d(src, fmt: int = FP4_NVFP4, rnd: int = FP4_RTN, seed: int = 0, in
     qt = QTensor(C, R, fmt, device=src.device)
     ready = False
     if amax_from is not None and fmt == FP4_NVFP4:
-        q.amax = amax_from.amax
+        q.amax = _amax_of(amax_from)
         ready = True
     if fmt == FP4_NVFP4:
         qt.amax = q.amax
@@ -646,7 +655,7 @@ def quantize(src, axis: int = FP4_AXIS_COLS, fmt: int = FP4_NVFP4, rnd: int = FP
     q = QTensor(rows, cols, fmt, device=src.device, had_signs=had_signs)
     ready = False
     if amax_from is not None and fmt == FP4_NVFP4:
-        q.amax = amax_from.amax
+        q.amax = _amax_of(amax_from)
         ready = True
     if noise is None:
         fp4_quantize(src, axis, rnd, seed, index_offset, ready, q, stream)
@@ -672,9 +681,9 @@ def quantize_dual(src, fmt: int = FP4_NVFP4, rnd_cols: int = FP4_RTN, seed_cols:
     two = fmt == FP4_NVFP4 and (qc.had_on or qr.had_on)
     if amax_from is not None and fmt == FP4_NVFP4:
         if two:
-            qc.amax, qr.amax = amax_from[0].amax, amax_from[1].amax
+            qc.amax, qr.amax = _amax_of(amax_from[0]), _amax_of(amax_from[1])
         else:
-            qc.amax = amax_from.amax
+            qc.amax = _amax_of(amax_from)
         ready = True
     if fmt == FP4_NVFP4 and not two:
         qr.amax = qc.amax
@@ -1042,10 +1051,10 @@ def _product(x, name: str):
     if not (c.is_cuda and c.device == s.device and c.dtype == s.dtype == torch.uint8 and c.is_contiguous()
             and s.is_contiguous() and rows > 0 and cols > 0 and cols % BLOCK[fmt] == 0 and c.numel() >= rows * cols // 2
             and s.numel() >= rows * cols // BLOCK[fmt]
-            and (not nv or (x.tscale.dtype == x.amax.dtype == torch.float32 and x.tscale.device == x.amax.device == c.device))):
+            and (not nv or (x.tscale.dtype == torch.float32 and x.tscale.device == c.device))):
         _check_qtensor(x, name)
-    d = fp4_tensor(c.data_ptr(), s.data_ptr(), x.amax.data_ptr() if nv else None, x.tscale.data_ptr() if nv else None,
-                   rows, cols, fmt, int(x.had_on), x.had_signs)
+    d = fp4_tensor(c.data_ptr(), s.data_ptr(), None, x.tscale.data_ptr() if nv else None, rows, cols, fmt, int(x.had_on),
+                   x.had_signs)   # a product reads no amax
     return fp4_operand(FP4_OPERAND_QUANTIZED, 0, ctypes.pointer(d)), d
 
 
