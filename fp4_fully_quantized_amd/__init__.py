@@ -272,6 +272,8 @@ def _check_qtensor(q, name: str, device=None, amax: bool = False):
     if q.fmt == FP4_NVFP4:
         if amax or q.amax is not None:
             _check_scalar(q.amax, f"{name}.amax", torch.float32, 1, device)
+            if amax and q.tscale is not None and q.amax.data_ptr() == q.tscale.data_ptr():
+                raise ValueError(f"{name}.amax and {name}.tscale are one tensor")
         _check_scalar(q.tscale, f"{name}.tscale", torch.float32, 1, device)
 
 

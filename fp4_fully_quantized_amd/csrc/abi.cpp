@@ -12,6 +12,7 @@
 #include "layer_checks.hpp"
 
 #include <cstdint>
+#include <initializer_list>
 
 // Workspace of fp4_gemm_noalloc: a device array each GPU holds from the
 // library's load until the process ends. Host code never uses this name as a
@@ -47,6 +48,15 @@ fp4_status check_matrix(const void* src, int dt, int64_t R, int64_t C, int64_t l
 
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
+// The tensor amax is read by every workgroup while one writes the tensor scale:
+// no output's amax is any output's tensor scale.
+fp4_status check_scalars(std::initializer_list<const fp4_tensor*> outs) {
+  for (const fp4_tensor* a : outs)
+    for (const fp4_tensor* b : outs)
+      if (a->fmt == FP4_NVFP4 && a->amax && a->amax == b->tscale) return FP4_ERR_UNSUPPORTED;
+  return FP4_OK;
+}
+
 // Every check of a single-orientation quantization, before anything is enqueued.
 fp4_status check_quant(const void* src, fp4_dtype src_t, int64_t R, int64_t C, int64_t ld, fp4_axis axis,
                        fp4_rounding rnd, uint64_t index_offset, const fp4_tensor* out) {
@@ -66,7 +76,7 @@ fp4_status check_quant(const void* src, fp4_dtype src_t, int64_t R, int64_t C, i
   if (rnd == FP4_SR && index_offset % 8 != 0) return FP4_ERR_ALIGN;
   if (axis == FP4_AXIS_ROWS && (R + 255) / 256 * ((C + 63) / 64) > 0x7FFFFFFF)
     return FP4_ERR_SHAPE;
-  return FP4_OK;
+  return check_scalars({out});
 }
 
 // Enqueue a quantization that check_quant accepted.
@@ -304,6 +314,8 @@ fp4_status quantize_dual_impl(const void* src, fp4_dtype src_t, int64_t R, int64
   if ((rnd_cols == FP4_SR && index_offset_cols % 8 != 0) || (rnd_rows == FP4_SR && index_offset_rows % 8 != 0))
     return FP4_ERR_ALIGN;
   if ((R + 127) / 128 * ((C + 127) / 128) > 0x7FFFFFFF) return FP4_ERR_SHAPE;
+  st = check_scalars({out_cols, out_rows});
+  if (st != FP4_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (nv && !amax_ready) {
     const bool bf = src_t == FP4_DTYPE_BF16;
@@ -604,6 +616,8 @@ fp4_status fp4_quantize_2d(const void* src, fp4_dtype src_t, int64_t R, int64_t 
   if (R % B != 0 || C % B != 0) return FP4_ERR_SHAPE;
   if (rnd == FP4_SR && index_offset % 8 != 0) return FP4_ERR_ALIGN;
   if ((R + 127) / 128 * ((C + 127) / 128) > 0x7FFFFFFF) return FP4_ERR_SHAPE;
+  st = check_scalars({out, out_t});
+  if (st != FP4_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (nv && !amax_ready) {
     fp4i_launch_amax(src, src_t == FP4_DTYPE_BF16, R, C, ld, out->amax, s);

@@ -97,8 +97,11 @@ typedef enum fp4_axis { FP4_AXIS_COLS = 0, FP4_AXIS_ROWS = 1 } fp4_axis;
  *   scales device, rows * cols / B bytes, row-major [rows][cols/B]
  *          (E4M3 bytes for NVFP4, E8M0 bytes for MXFP4)
  *   amax   device FP32 scalar: the tensor amax (NVFP4; NULL for MXFP4)
- *   tscale device FP32 scalar: the tensor scale s_g (NVFP4; NULL for MXFP4)
- * codes and scales must be 16-byte aligned. */
+ *   tscale device FP32 scalar: the tensor scale s_g (NVFP4; NULL for MXFP4); a
+ *          scalar of its own: a quantization whose outputs' amax and tscale share
+ *          one is refused (FP4_ERR_UNSUPPORTED)
+ * codes and scales must be 16-byte aligned. Products and dequantizations do not
+ * read amax (it may be NULL there). */
 typedef struct fp4_tensor {
     uint8_t* codes;
     uint8_t* scales;

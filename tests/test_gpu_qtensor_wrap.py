@@ -59,7 +59,8 @@ def test_wrap_without_amax_is_no_amax(fp4):
 
 
 def test_wrap_as_an_output(fp4):
-    """A tensor without an amax is not quantized into; one with an amax and a tensor scale of its own is."""
+    """An output has an amax and a tensor scale of its own: neither a tensor without an amax nor one whose amax is its
+    tensor scale is quantized into (one kernel reads the one while it writes the other)."""
     import torch
     say("wrap as an output")
     x = rand(4, 64, 512)
@@ -71,8 +72,9 @@ def test_wrap_as_an_output(fp4):
 
     def into(q):
         fp4.fp4_quantize(x, fp4.FP4_AXIS_COLS, fp4.FP4_RTN, 0, 0, False, q)
-    with pytest.raises(ValueError, match="amax"):
-        into(out(tscale=s))
+    for bad in (out(tscale=s), out(amax=s, tscale=s)):
+        with pytest.raises(ValueError, match="amax"):
+            into(bad)
     good = out(amax=s, tscale=t)
     into(good)
     assert torch.equal(good.codes, want.codes) and torch.equal(t, want.tscale) and torch.equal(s, want.amax)
