@@ -1053,7 +1053,7 @@ def _product(x, name: str):
     if not (c.is_cuda and c.device == s.device and c.dtype == s.dtype == torch.uint8 and c.is_contiguous()
             and s.is_contiguous() and rows > 0 and cols > 0 and cols % BLOCK[fmt] == 0 and c.numel() >= rows * cols // 2
             and s.numel() >= rows * cols // BLOCK[fmt]
-            and (not nv or (x.tscale.dtype == torch.float32 and x.tscale.device == c.device))):
+            and (not nv or (getattr(x.tscale, "dtype", None) == torch.float32 and x.tscale.device == c.device))):
         _check_qtensor(x, name)
     d = fp4_tensor(c.data_ptr(), s.data_ptr(), None, x.tscale.data_ptr() if nv else None, rows, cols, fmt, int(x.had_on),
                    x.had_signs)   # a product reads no amax

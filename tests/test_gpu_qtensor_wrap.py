@@ -78,3 +78,13 @@ def test_wrap_as_an_output(fp4):
     good = out(amax=s, tscale=t)
     into(good)
     assert torch.equal(good.codes, want.codes) and torch.equal(t, want.tscale) and torch.equal(s, want.amax)
+
+
+def test_wrap_without_tensor_scale(fp4):
+    """An NVFP4 operand without its tensor scale is refused as every other argument is."""
+    say("wrap without a tensor scale")
+    q = fp4.quantize(rand(5, 64, 512))
+    w = fp4.QTensor.wrap(q.codes, q.scales, fp4.FP4_NVFP4)
+    for call in (lambda: fp4.gemm(w, q), lambda: fp4.gemm_fused(w, q), lambda: fp4.gemm_fused(q, w), lambda: fp4.dequantize(w)):
+        with pytest.raises(ValueError, match="tscale"):
+            call()
