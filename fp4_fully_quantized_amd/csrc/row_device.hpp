@@ -214,14 +214,21 @@ struct Mx8In {
 };
 
 // Stores the chunk at column c of row r in 8 bits. The four lanes of a block
-// call it together (zeros past the last column); a lane whose block lies past
-// the row stores nothing. Returns the scale byte.
+// call it together (zeros, or NaN, past the last column); a lane whose block lies
+// past the row stores nothing. Returns the scale byte.
 template <bool NT = false>
 __device__ __forceinline__ uint32_t mx8_store(const Mx8Out& q, int64_t r, uint32_t c, uint32_t n, const float x[8],
                                               uint32_t& block_mag) {
   block_mag = quad_max(__float_as_uint(number_max8(x)));
   const uint32_t byte = mx8_byte(block_mag);
-  const uint2 w = mx8_pack8(x, mx8_factor(byte));
+  uint2 w = mx8_pack8(x, mx8_factor(byte));
+  if (c + 8 > n) {
+    // Codes past the last column are zeros whatever x holds there (a norm's row whose
+    // rstd is not finite) and whatever its factor is (byte 255's NaN).
+    const uint32_t k = n > c ? n - c : 0;
+    w.x &= k >= 4 ? ~0u : (1u << 8 * k) - 1;
+    w.y &= k >= 4 ? (1u << 8 * (k - 4)) - 1 : 0u;
+  }
   if ((c & ~31u) < n) {
     v2u* const d = reinterpret_cast<v2u*>(q.codes + r * q.ld + c);
     if constexpr (NT) __builtin_nontemporal_store((v2u){w.x, w.y}, d);

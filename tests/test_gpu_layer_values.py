@@ -103,3 +103,47 @@ def test_norm_checkpoint_of_nan(fp4, cols):
     o = fp4.rmsnorm(x, torch.ones(cols, device="cuda"), residual=r, h8=True)
     check_mx8(o.h8, host(x + r), "h8")
     assert np.array_equal(np.isnan(host(fp4.mx8_dequantize(o.h8))), np.isnan(host(x + r)))
+
+
+# ---------------------------------------------------------------- padding
+@pytest.mark.parametrize("cols", [1, 40, 300, 5003, 20001])
+def test_norm_pads_stay_zero(fp4, cols):
+    """The codes past a row's last column are zeros also where the row's rstd is not finite: a NaN or an infinity in
+    the row, a row of zeros with eps = 0."""
+    import torch
+    say("norm pads", cols)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    x = torch.randn((5, cols), generator=gen, device="cuda")
+    x[1, 0] = float("nan")
+    x[2] = 0
+    x[3, cols - 1] = float("inf")
+    g = torch.ones(cols, device="cuda")
+    for residual in (None, torch.zeros_like(x)):
+        o = fp4.rmsnorm(x, g, eps=0.0, residual=residual, y8=True, h8=True)
+        assert torch.isnan(o.y[1:3]).all() and torch.isfinite(o.y[[0, 4]]).all()
+        for q, v in ((o.y8, o.y), (o.h8, x)):
+            assert not q.codes[:, cols:].any()
+            for r in (0, 1, 2, 4):   # the infinity's block stands for NaN whatever its codes
+                codes, scales = ref.mx8_encode(host(v[r:r + 1]))
+                assert np.array_equal(q.scales[r:r + 1].cpu().numpy(), scales)
+                equal_codes(q.codes[r:r + 1].cpu().numpy(), codes)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [1, 40, 91, 2501])
+def test_pads_of_a_block_with_an_infinity(fp4, kind, cols):
+    """Zeros there too: in a matrix's 8-bit form, and in a product's checkpoint."""
+    import torch
+    say("pads, infinity", kind, cols)
+    x = torch.ones((9, cols), device="cuda").to({"bf16": torch.bfloat16, "f32": torch.float32}[kind])
+    x[::2, cols - 1] = float("inf")
+    q = fp4.mx8_quantize(x)
+    assert not q.codes[:, cols:].any() and (q.scales[::2, -1] == 255).all()
+    assert torch.isnan(fp4.mx8_dequantize(q)[::2, cols - 1]).all()
+    for rows in (9, 2500):   # the kernel of few tiles, and the tiled one's edges
+        A, B = fp4.quantize(torch.ones((rows, 256), device="cuda")), fp4.quantize(torch.ones((cols, 256), device="cuda"))
+        b = torch.zeros(cols, device="cuda")
+        b[cols - 1] = float("inf")
+        _, z = fp4.gemm_fused(A, B, bias=b, checkpoint=True)
+        assert not z.codes[:, cols:].any() and (z.scales[:, -1] == 255).all()
