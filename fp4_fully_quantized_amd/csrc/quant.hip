@@ -66,6 +66,9 @@ __device__ __forceinline__ void hadamard16_lane_pair(float x[8], uint32_t signs,
   for (int i = 0; i < 8; ++i) x[i] = x[i] * 0.25f;
 }
 
+// |x|; a signalling NaN quiet, so that a maximum of it and a number is the number.
+__device__ __forceinline__ float magnitude(float x) { return fabsf(__builtin_canonicalizef(x)); }
+
 // Wave and workgroup max of m >= 0, then at most one atomicMax per workgroup
 // on the float bits (monotone for non-negative floats). The value at *amax
 // only grows, so a workgroup whose max does not exceed a value read from it
@@ -120,7 +123,7 @@ __global__ __launch_bounds__(256) void k_amax(const void* __restrict__ src, int6
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[k][i]));
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, magnitude(x[k][i]));
   }
   amax_reduce(m, amax);
 }
@@ -129,7 +132,10 @@ __global__ __launch_bounds__(256) void k_amax(const void* __restrict__ src, int6
 // over its 16-byte pieces with four nontemporal loads in flight per lane, the
 // maximum taken on the magnitude bits (|x| of a finite float, bf16 or fp32,
 // orders as its bit pattern with the sign cleared, an unsigned integer): bf16
-// pairs by a packed 16-bit unsigned max, fp32 by a 32-bit one; exact.
+// pairs by a packed 16-bit unsigned max, fp32 by a 32-bit one; exact. A NaN's bits
+// are above every number's, so a lane that ends with one takes its pieces again as
+// floats, NaN left out as k_amax leaves it out (inside the main loop that took 1.3
+// to 2.5% more of the pass: 32768 x 11008 bf16 108.7 us against 106.2).
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_amax_flat(const v4u* __restrict__ src, uint64_t n16, float* amax) {
   const uint64_t stride = (uint64_t)gridDim.x * blockDim.x;
@@ -160,12 +166,24 @@ __global__ __launch_bounds__(256) void k_amax_flat(const v4u* __restrict__ src, 
     take(x3);
   }
   for (; i < n16; i += stride) take(__builtin_nontemporal_load(src + i));
-  float m;
+  uint32_t top;
   if constexpr (BF16) {
     const v2us q = __builtin_elementwise_max(p0, p1);
-    m = __uint_as_float((uint32_t)max(q.x, q.y) << 16);
+    top = (uint32_t)max(q.x, q.y) << 16;
   } else {
-    m = __uint_as_float(max(m0, m1));
+    top = max(m0, m1);
+  }
+  float m = __uint_as_float(top);
+  if (top > 0x7F800000u) {
+    m = 0.0f;
+    for (i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16; i += stride) {
+      const v4u v = src[i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (BF16) m = fmaxf(m, magnitude(bf16_lo(v[k])));
+        m = fmaxf(m, magnitude(BF16 ? bf16_hi(v[k]) : __uint_as_float(v[k])));
+      }
+    }
   }
   amax_reduce(m, amax);
 }
@@ -531,7 +549,7 @@ __global__ __launch_bounds__(256) void k_amax_pair(const void* __restrict__ src,
       for (int j = 0; j < 8; ++j) w[j] = x[i][j];
       if constexpr (HC) hadamard16_lane_pair(w, signs_c, lane & 1);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mc = fmaxf(mc, fabsf(w[j]));
+      for (int j = 0; j < 8; ++j) mc = fmaxf(mc, magnitude(w[j]));
     }
     // blocks along R
     if constexpr (HR) {
@@ -548,7 +566,7 @@ __global__ __launch_bounds__(256) void k_amax_pair(const void* __restrict__ src,
 #pragma unroll
       for (int i = 0; i < 16; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mr = fmaxf(mr, fabsf(x[i][j]));
+        for (int j = 0; j < 8; ++j) mr = fmaxf(mr, magnitude(x[i][j]));
     }
   }
   amax_reduce(mc, amax_c);

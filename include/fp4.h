@@ -128,7 +128,8 @@ uint32_t fp4_hadamard_signs(uint64_t seed);
 const char* fp4_status_str(fp4_status s);
 
 /* Tensor amax: *amax = max |x| over the R x C matrix src (row-major, leading
- * dimension ld elements, FP32 or bf16; device). amax is a device FP32 scalar.
+ * dimension ld elements, FP32 or bf16; device), NaN left out (0 if there is no
+ * other value). amax is a device FP32 scalar.
  * The NVFP4 tensor scale depends on it (Robots Atlas "FP4", How it works:
  * the per-tensor FP32 scale). Requires R, C >= 1, C % 8 == 0, ld >= C,
  * ld % 8 == 0, src 16-byte aligned. */

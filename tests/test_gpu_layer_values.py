@@ -147,3 +147,35 @@ def test_pads_of_a_block_with_an_infinity(fp4, kind, cols):
         b[cols - 1] = float("inf")
         _, z = fp4.gemm_fused(A, B, bias=b, checkpoint=True)
         assert not z.codes[:, cols:].any() and (z.scales[:, -1] == 255).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 8), (3, 2048), (700, 4096)])
+def test_tensor_amax_with_nan(fp4, rows, cols, kind):
+    """The largest magnitude of the values that are no NaN, of a contiguous matrix as of a strided one: a NaN hides
+    none of the values beside it."""
+    import torch
+    say("tensor amax with NaN", rows, cols, kind)
+    t = {"bf16": torch.bfloat16, "f32": torch.float32}[kind]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(9)
+    wide = torch.randn((rows, cols + 8), generator=gen, device="cuda").to(t)
+    bits = wide.view(torch.int16 if kind == "bf16" else torch.int32)
+    shift = 0 if kind == "bf16" else 16
+    r = rows // 2
+    wide[r, 3] = -1000.0
+    bits[r, 4:6] = 0x7FC0 << shift
+    bits[r, 6] = 0x7F81 << shift    # signalling
+    bits[r, 7] = (0xFFFF - 0x10000) << shift
+    out = torch.empty(1, device="cuda")
+    for src in (wide[:, :cols], wide[:, :cols].contiguous()):
+        fp4.fp4_tensor_amax(src, out)
+        assert float(out) == 1000.0
+    for big in (float("inf"), float("-inf")):
+        wide[r, 3] = big
+        for src in (wide[:, :cols], wide[:, :cols].contiguous()):
+            fp4.fp4_tensor_amax(src, out)
+            assert float(out) == float("inf")
+    wide[:] = float("nan")
+    fp4.fp4_tensor_amax(wide[:, :cols].contiguous(), out)
+    assert float(out) == 0.0
