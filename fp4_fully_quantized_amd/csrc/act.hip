@@ -1,6 +1,6 @@
 // act.hip -- the gradient of the product's epilogue: dz = dy act'(z), the
-// bias's gradient (the column sums of dz) and max |dz|, in one pass that is
-// bound by HBM (2 + 2 + 1 + 1/32 bytes per bf16 value with z in 8 bits).
+// bias's gradient (the column sums of dz) and max |dz| (NaN left out), in one pass
+// that is bound by HBM (2 + 2 + 1 + 1/32 bytes per bf16 value with z in 8 bits).
 //
 // A workgroup takes a slab of 256 columns over a range of rows: 32 lanes along
 // the columns (chunks of 8), 8 along the rows, kUnroll rows of each lane in
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(256) void k_act_bwd(Act a) {
         d[i] *= z[i];
         acc[i] += d[i];
       }
-      top = max(top, mag_max8_stored<BF16>(d));
+      top = max(top, number_max8_bits(d));
       if (r < last && c < a.cols) store_chunk<BF16, NT>(a.dz + r * a.ld_dz * ES, c, a.cols, d);
       // One row's values at a time in registers (all at once took 140).
       __builtin_amdgcn_sched_barrier(0);
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void k_act_bwd(Act a) {
     }
   }
   if (a.max_part) {
-    top = wave_max(top);
+    top = wave_max(BF16 ? bf16_bits(top) : top);  // of the values as stored
     if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
     __syncthreads();
     if (threadIdx.x == 0)

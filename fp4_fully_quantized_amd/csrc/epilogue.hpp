@@ -88,7 +88,7 @@ struct EpiWhole {
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = __builtin_fmaf(z[i], alpha, bias[i]);
     if (e.z8.codes) {
-      const uint32_t byte = fp4row::mx8_byte(fp4row::quad_max(__float_as_uint(fp4row::number_max8(z))));
+      const uint32_t byte = fp4row::mx8_byte(fp4row::quad_max(fp4row::number_max8_bits(z)));
       const uint2 w = fp4row::mx8_pack8(z, fp4row::mx8_factor(byte));
       __builtin_nontemporal_store((fp4row::v2u){w.x, w.y}, reinterpret_cast<fp4row::v2u*>(codes));
       if (first) *scales = (uint8_t)byte;

@@ -79,7 +79,8 @@ struct Fwd {
 };
 
 // The outputs of one chunk of a row whose h and rstd are known. Returns the
-// largest magnitude of the stored y.
+// largest magnitude of y as it is stored, NaN left out; of a bf16 y that before
+// the rounding (stored_max).
 template <bool BF16, bool NT>
 __device__ __forceinline__ uint32_t norm_out(const Fwd& a, int64_t r, uint32_t c, const float h[8], const float g[8],
                                              float rstd) {
@@ -92,19 +93,26 @@ __device__ __forceinline__ uint32_t norm_out(const Fwd& a, int64_t r, uint32_t c
   for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * g[i];
   if (a.y8.codes) {
     const uint32_t byte = mx8_store<NT>(a.y8, r, c, a.cols, y, m);
-    if (a.amax && !a.y) {
-      // The block's largest stored value: rounding keeps the order.
+    if (a.amax && !a.y && byte != 255) {
+      // The block's largest stored value: rounding keeps the order. A block with an
+      // infinity stands for NaN, and is left out as one.
       const float one[8] = {__uint_as_float(m), 0, 0, 0, 0, 0, 0, 0};
       float v[8];
       mx8_unpack8(mx8_pack8(one, mx8_factor(byte)), mx8_scale(byte), v);
-      top = __float_as_uint(v[0]) & 0x7FFFFFFFu;
+      top = __float_as_uint(v[0]);
     }
   }
   if (a.y && c < a.cols) {
     store_chunk<BF16, NT>(a.y + r * a.ld_y * ES, c, a.cols, y);
-    if (a.amax) top = mag_max8_stored<BF16>(y);
+    if (a.amax) top = number_max8_bits(y);
   }
   return top;
+}
+
+// The maximum over norm_out's results as the stored values' own.
+template <bool BF16>
+__device__ __forceinline__ uint32_t stored_max(const Fwd& a, uint32_t top) {
+  return BF16 && a.y ? bf16_bits(top) : top;
 }
 
 // A lane's part of one row as it lies in memory (zeros from row a.rows on).
@@ -165,7 +173,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void k_norm(Fwd a) {
 #pragma unroll
     for (int k = 0; k < NCH; ++k) top = max(top, norm_out<BF16, NT>(a, r, (k * T + t) * 8, h[k], g[k], rstd));
   }
-  if (a.amax) amax_out<BLOCK>(top, a.amax);
+  if (a.amax) amax_out<BLOCK>(stored_max<BF16>(a, top), a.amax);
 }
 
 // Rows of any length: one for the sum, once more for the outputs.
@@ -205,7 +213,7 @@ __global__ __launch_bounds__(1024) void k_norm_long(Fwd a) {
       top = max(top, norm_out<BF16, false>(a, r, c, h, g, rstd));
     }
   }
-  if (a.amax) amax_out<T>(top, a.amax);
+  if (a.amax) amax_out<T>(stored_max<BF16>(a, top), a.amax);
 }
 
 struct Bwd {

@@ -134,14 +134,6 @@ __device__ __forceinline__ void store_chunk(char* p, uint32_t c, uint32_t n, con
   }
 }
 
-// max |x| as a bit pattern: magnitudes of floats order as unsigned integers, an
-// infinity or a NaN above every finite one, so none is lost on the way.
-__device__ __forceinline__ uint32_t mag_max8(const float x[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  return m;
-}
 // max |x| over the values that are no NaN, 0 if none (the maximum of a number and a
 // NaN is the number, so it starts from one; the sign is dropped for free, unlike in
 // integers). A signalling NaN, which only memory can hold, is made quiet first: the
@@ -152,17 +144,11 @@ __device__ __forceinline__ float number_max8(const float x[8]) {
   for (int i = 0; i < 8; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(__builtin_canonicalizef(x[i])));
   return m;
 }
-// The same of the values as bf16 stores them.
-template <bool BF16>
-__device__ __forceinline__ uint32_t mag_max8_stored(const float x[8]) {
-  if constexpr (!BF16) return mag_max8(x);
-  typedef unsigned short v2us __attribute__((ext_vector_type(2)));
-  v2us m = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    m = __builtin_elementwise_max(m, __builtin_bit_cast(v2us, pack_bf16(x[2 * i], x[2 * i + 1]) & 0x7FFF7FFFu));
-  return (uint32_t)max(m.x, m.y) << 16;
-}
+// The bits of that maximum: magnitudes of floats order as unsigned integers.
+__device__ __forceinline__ uint32_t number_max8_bits(const float x[8]) { return __float_as_uint(number_max8(x)); }
+// A maximum of values as bf16 stores them, from that of the values (rounding keeps
+// the order).
+__device__ __forceinline__ uint32_t bf16_bits(uint32_t m) { return pack_bf16(0.0f, __uint_as_float(m)) & 0xFFFF0000u; }
 
 // ---- 8 bits: E4M3 values, one E8M0 byte per 32 -----------------------------
 __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
@@ -219,7 +205,7 @@ struct Mx8In {
 template <bool NT = false>
 __device__ __forceinline__ uint32_t mx8_store(const Mx8Out& q, int64_t r, uint32_t c, uint32_t n, const float x[8],
                                               uint32_t& block_mag) {
-  block_mag = quad_max(__float_as_uint(number_max8(x)));
+  block_mag = quad_max(number_max8_bits(x));
   const uint32_t byte = mx8_byte(block_mag);
   uint2 w = mx8_pack8(x, mx8_factor(byte));
   if (c + 8 > n) {

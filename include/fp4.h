@@ -468,7 +468,8 @@ fp4_status fp4_gemm_noalloc(const fp4_operand* A, const fp4_operand* B, fp4_dtyp
  * used throughout: every sum, statistic and intermediate value; each output is
  * rounded once, to nearest even, when it is stored. Sums over rows are added in
  * a fixed order that depends on the shape alone, so results do not change
- * between runs. Infinities and NaN propagate as in FP32 arithmetic. */
+ * between runs. Infinities and NaN propagate as in FP32 arithmetic; a maximum
+ * (amax, a block's scale) leaves NaN out. */
 
 /* A rows x cols matrix in 8 bits: E4M3 values with one E8M0 scale byte for each
  * block of 32 consecutive values of a row (the last block of a row may be
@@ -517,8 +518,9 @@ fp4_status fp4_mx8_dequantize(const fp4_mx8* q, fp4_dtype dst_t, void* dst, int6
  *             fp4_rmsnorm_backward reads).
  *   rstd      NULL, or device, rows FP32 values (the backward pass needs them).
  *   amax      NULL, or a device FP32 scalar: max |y| over the stored values (y's
- *             when y is given, else y8's): what fp4_quantize* take with
- *             amax_ready = 1 for these values (without a rotation).
+ *             when y is given, else y8's) as fp4_tensor_amax takes it, NaN left
+ *             out: what fp4_quantize* take with amax_ready = 1 for these values
+ *             (without a rotation).
  * At least one of h, y, y8, h8 is given. Outputs may be the inputs' own buffers
  * (h or y = x or residual, with its leading dimension).
  * Errors: FP4_ERR_NULL (x, gamma, no output), FP4_ERR_ARG (dtypes; eps negative
@@ -626,8 +628,9 @@ fp4_status fp4_gemm_fused(const fp4_operand* A, const fp4_operand* B, const fp4_
  *   z / z8  exactly one of them: the pre-activation, or its 8-bit form.
  *   dz      may be dy's own buffer, with its leading dimension.
  *   dbias   device, cols FP32 values, or NULL.
- *   amax    a device FP32 scalar, or NULL: max |dz| over the stored values, what
- *           fp4_quantize* take with amax_ready = 1 for dz (without a rotation).
+ *   amax    a device FP32 scalar, or NULL: max |dz| over the stored values as
+ *           fp4_tensor_amax takes it, NaN left out: what fp4_quantize* take with
+ *           amax_ready = 1 for dz (without a rotation).
  *   ws      device, 256-byte aligned, at least
  *           fp4_act_backward_workspace_bytes(rows, cols) bytes; not needed
  *           (NULL) when that is 0 or neither dbias nor amax is asked for.

@@ -149,6 +149,64 @@ def test_pads_of_a_block_with_an_infinity(fp4, kind, cols):
         assert not z.codes[:, cols:].any() and (z.scales[:, -1] == 255).all()
 
 
+# ---------------------------------------------------------------- amax
+def largest(v):
+    """max |v| over the values that are no NaN (0 if none)."""
+    a = np.abs(host(v))
+    return float(np.where(np.isnan(a), 0.0, a).max())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 40), (6, 500), (37, 4096), (1500, 1003), (5, 20000)])
+def test_norm_amax_with_nan(fp4, rows, cols, kind):
+    """amax is max |y| over the stored values that are no NaN, whether y or its 8-bit form is stored: what quantize's
+    own pass over them finds."""
+    import torch
+    say("norm amax with NaN", rows, cols, kind)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    x = torch.randn((rows, cols), generator=gen, device="cuda").to({"bf16": torch.bfloat16, "f32": torch.float32}[kind])
+    g = torch.randn(cols, generator=gen, device="cuda")
+    for where in ("gamma", "row", "all", "infinity"):
+        xx, gg = x.clone(), g.clone()
+        if where == "gamma":
+            gg[3] = float("nan")
+        elif where == "row":
+            xx[rows // 2, 7] = float("nan")
+        elif where == "all":
+            gg[:] = float("nan")
+        else:
+            gg[5] = float("inf")
+        for y, y8 in ((True, False), (False, True), (True, True)):
+            o = fp4.rmsnorm(xx, gg, y=y, y8=y8, amax=True)
+            stored = o.y if y else fp4.mx8_dequantize(o.y8)
+            assert float(o.amax) == largest(stored), (where, y, y8)
+        if cols % 16 == 0 and where in ("gamma", "row", "all"):
+            n = fp4.rmsnorm(xx, gg, amax=True)
+            a, b = fp4.quantize(n.y, amax_from=n), fp4.quantize(n.y)
+            assert torch.equal(a.amax, b.amax) and torch.equal(a.tscale, b.tscale), where
+            assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales), where
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 40), (70, 1001), (513, 2504)])
+def test_act_backward_amax_with_nan(fp4, rows, cols, kind):
+    import torch
+    say("act backward amax with NaN", rows, cols, kind)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    t = {"bf16": torch.bfloat16, "f32": torch.float32}[kind]
+    z = torch.randn((rows, cols), generator=gen, device="cuda").to(t)
+    dy = torch.randn((rows, cols), generator=gen, device="cuda").to(t)
+    for act in (0, 1, 2, 3):
+        for bad in (float("nan"), float("inf")):
+            d = dy.clone()
+            d[rows // 2, 8:17] = bad
+            z[rows // 2, 8:17] = 1.0
+            o = fp4.act_backward(d, z, act, amax=True)
+            assert float(o.amax) == largest(o.dz), (act, bad)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,cols", [(1, 8), (3, 2048), (700, 4096)])
 def test_tensor_amax_with_nan(fp4, rows, cols, kind):
