@@ -46,6 +46,7 @@ fp4_status fp4_mx8_dequantize(const fp4_mx8* q, fp4_dtype dst_t, void* dst, int6
 
 fp4_status fp4_rmsnorm(const fp4_rmsnorm_fwd* n, fp4_stream_t stream) {
   if (!n || !n->x || !n->gamma || !(n->h || n->y || n->y8 || n->h8)) return FP4_ERR_NULL;
+  if (n->amax && !n->y && !n->y8) return FP4_ERR_NULL;  // of no stored values
   if (!dtype_ok(n->dtype) || !dtype_ok(n->gamma_t)) return FP4_ERR_ARG;
   if (!(n->eps >= 0.0f) || std::isinf(n->eps)) return FP4_ERR_ARG;
   const int64_t R = n->rows, C = n->cols;

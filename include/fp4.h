@@ -520,7 +520,7 @@ fp4_status fp4_mx8_dequantize(const fp4_mx8* q, fp4_dtype dst_t, void* dst, int6
  *   amax      NULL, or a device FP32 scalar: max |y| over the stored values (y's
  *             when y is given, else y8's) as fp4_tensor_amax takes it, NaN left
  *             out: what fp4_quantize* take with amax_ready = 1 for these values
- *             (without a rotation).
+ *             (without a rotation). Needs y or y8 (FP4_ERR_NULL).
  * At least one of h, y, y8, h8 is given. Outputs may be the inputs' own buffers
  * (h or y = x or residual, with its leading dimension).
  * Errors: FP4_ERR_NULL (x, gamma, no output), FP4_ERR_ARG (dtypes; eps negative
