@@ -12,10 +12,11 @@ inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintpt
 inline bool dtype_ok(int t) { return t == FP4_DTYPE_F32 || t == FP4_DTYPE_BF16; }
 inline bool act_ok(int a) { return a >= FP4_ACT_NONE && a <= FP4_ACT_SILU; }
 
-// Rows and columns each index a launch dimension or a lane's 32-bit column;
-// offsets into a matrix are 64-bit.
+// Rows and columns each index a launch dimension or a lane's 32-bit column (its byte
+// offset too); offsets into a matrix are 64-bit. 2^25 columns are more than any
+// product has: its operands' codes stay below 2^31 bytes and its K is at least 128.
 inline bool dims_ok(int64_t rows, int64_t cols) {
-  return rows >= 1 && cols >= 1 && rows <= INT32_MAX && cols <= (int64_t(1) << 24);
+  return rows >= 1 && cols >= 1 && rows <= INT32_MAX && cols <= (int64_t(1) << 25);
 }
 
 // A rows x cols matrix of dt (valid) with leading dimension ld.

@@ -463,8 +463,9 @@ fp4_status fp4_gemm_noalloc(const fp4_operand* A, const fp4_operand* B, fp4_dtyp
  * root-mean-square norm that feeds them, an epilogue on the product itself, and
  * 8-bit checkpoints of what their backward passes read.
  *
- * These calls take any rows, cols >= 1 and any leading dimension >= cols, and
- * matrices aligned to their element size only; 8-bit tensors as below. FP32 is
+ * These calls take any rows from 1 to 2^31 - 1 and cols from 1 to 2^25 (every
+ * width a product can have; FP4_ERR_SHAPE beyond), any leading dimension >= cols,
+ * and matrices aligned to their element size only; 8-bit tensors as below. FP32 is
  * used throughout: every sum, statistic and intermediate value; each output is
  * rounded once, to nearest even, when it is stored. Sums over rows are added in
  * a fixed order that depends on the shape alone, so results do not change

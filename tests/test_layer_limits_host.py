@@ -27,3 +27,11 @@ def test_norm_amax_without_y(fp4):
     for outputs in ({"h": P, "ld_h": 40}, {"h8": ctypes.pointer(q)}, {"h": P, "ld_h": 40, "h8": ctypes.pointer(q)}):
         n = fp4.fp4_rmsnorm_fwd(rows=4, cols=40, dtype=0, gamma_t=0, x=P, ld_x=40, gamma=P, amax=P, eps=1e-5, **outputs)
         assert fp4.lib().fp4_rmsnorm(ctypes.byref(n), None) == NULL, outputs
+
+
+def test_widths_past_every_product(fp4):
+    """2^25 columns are taken (as wide as a product goes), more are not."""
+    L, n = fp4.lib(), (1 << 25) + 1
+    assert L.fp4_mx8_quantize(P, 0, n, ctypes.byref(fp4.fp4_mx8(P, P, 1, n, n + 31, n // 32 + 1)), None) == 2
+    assert fp4.fp4_act_backward_workspace_bytes(2000, n) == 0 < fp4.fp4_act_backward_workspace_bytes(2000, n - 1)
+    assert fp4.fp4_rmsnorm_backward_workspace_bytes(2, n) == 0 < fp4.fp4_rmsnorm_backward_workspace_bytes(2, n - 1)
