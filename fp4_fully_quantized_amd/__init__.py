@@ -747,7 +747,7 @@ def _fast_raw_stream():
 
 def _raw(stream, device):
     """The stream's handle for a call on device, which must be the current one (a launch goes there)."""
-    global _raw, _current_device
+    global _raw
     import torch
     fast, current = _fast_raw_stream(), torch.cuda.current_device
 
