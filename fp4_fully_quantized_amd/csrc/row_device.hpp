@@ -67,10 +67,6 @@ __device__ __forceinline__ Raw8<BF16> raw8_any(const char* p) {
   }
   return r;
 }
-template <bool BF16>
-__device__ __forceinline__ void load8_any(const char* p, float x[8]) {
-  expand<BF16>(raw8_any<BF16>(p), x);
-}
 
 // Columns c .. c + 7 of the row at p, zeros from column n on.
 template <bool BF16, bool NT = false>
