@@ -49,13 +49,14 @@ def copy(reps: int = 3) -> None:
 
 # The operators around the product at the sizes the documents quote, in launch
 # order: (label, kernel name regex of its main launch, bytes it cannot do without,
-# flops).
+# flops). The last of them are too small to fill the chip, or have a path of their own.
 LAYER_REPS = 20
 LAYER_COMMAND = ("rocprofv3 --kernel-trace --stats --output-format csv -d OUT/prof_layer -o layer -- "
                  "python3 -m fp4_fully_quantized_amd.profiling layer")
 _E8 = 1 + 1 / 32
 LAYER_DISPATCHES = [
     ("norm 32768 x 4096 bf16: residual, y and h in 8 bits, amax", r"^k_norm<", 32768 * 4096 * (6 + 2 * _E8), 0),
+    ("norm 32768 x 4096 bf16: residual, y in bf16, h in 8 bits, amax", r"^k_norm<", 32768 * 4096 * (8 + _E8), 0),
     ("norm backward 32768 x 4096 bf16, from 8 bits, residual's gradient", r"^k_norm_bwd<", 32768 * 4096 * (6 + _E8), 0),
     ("act backward 4096 x 11008 bf16, GELU, from 8 bits", r"^k_act_bwd<", 4096 * 11008 * (4 + _E8), 0),
     ("16384 x 8192 bf16 to 8 bits", r"^k_mx8_quant<", 16384 * 8192 * (2 + _E8), 0),
@@ -64,39 +65,67 @@ LAYER_DISPATCHES = [
      (32768 + 11008) * 4096 * 0.5625 + 32768 * 11008 * (2 + _E8), 2.0 * 32768 * 11008 * 4096),
     ("MXFP4 product 4096 x 4096 x 11008, bias, residual, fp32 out", r"^k_gemm_mx8_epi<",
      8192 * 11008 * 0.53125 + 4096 * 4096 * 8, 2.0 * 4096 * 4096 * 11008),
-    ("NVFP4 product 512 x 4096 x 4096, bias, SILU, bf16 out", r"^k_gemm_rows<0,",
-     (512 + 4096) * 4096 * 0.5625 + 512 * 4096 * 2, 2.0 * 512 * 4096 * 4096),
+    *((f"NVFP4 product {m} x 4096 x 4096, bias, SILU, bf16 out", r"^k_gemm_rows<0,",
+       (m + 4096) * 4096 * 0.5625 + m * 4096 * 2, 2.0 * m * 4096 * 4096) for m in (128, 512, 1024)),
     ("NVFP4 product 1 x 11008 x 4096, bias, SILU, bf16 out", r"^k_gemm_rows<0,",
      (1 + 11008) * 4096 * 0.5625 + 11008 * 2, 2.0 * 11008 * 4096),
     ("MXFP4 product 24 x 4096 x 11008, residual, bf16 out", r"^k_gemm_rows<1,",
      (24 + 4096) * 11008 * 0.53125 + 24 * 4096 * 4, 2.0 * 24 * 4096 * 11008),
+    ("norm 1 x 4096 bf16: residual, y, amax", r"^k_norm<", 4096 * 8 + 4096 * 4, 0),
+    ("norm backward 333 x 1003 fp32", r"^k_norm_bwd<", 333 * 1003 * 12, 0),
+    ("act backward 200 x 1001 fp32, SILU", r"^k_act_bwd<", 200 * 1001 * 12, 0),
+    ("1000 x 2504 fp32 from 8 bits", r"^k_mx8_dequant<", 1000 * 2504 * (4 + _E8), 0),
+    ("norm backward 8192 x 11008 fp32", r"^k_norm_bwd<", 8192 * 11008 * 12, 0),
+    ("norm backward 4096 x 16384 fp32", r"^k_norm_bwd<", 4096 * 16384 * 12, 0),
+    ("norm backward 4096 x 16384 bf16, from 8 bits", r"^k_norm_bwd<", 4096 * 16384 * (4 + _E8), 0),
 ]
 
 
 def layer(reps: int = LAYER_REPS) -> None:
-    """Each operator of LAYER_DISPATCHES `reps` times, over three sets of inputs in turn."""
+    """Each operator of LAYER_DISPATCHES `reps` times, over three sets of inputs in turn; products of few rows over
+    `reps` weight matrices, each read once and from memory, as a serving loop reads its layers (three of them would
+    stay in the 256 MiB cache)."""
     import torch
 
     import fp4_fully_quantized_amd as fp4
 
-    bf = torch.bfloat16
+    bf, f32 = torch.bfloat16, torch.float32
 
     def rand(*shape, n=3, dtype=bf, scale=1.0):
         return [(torch.randn(shape, device="cuda") * scale).to(dtype) for _ in range(n)]
 
     def product(fmt, m, n, k, bias, act, residual, checkpoint, dtype):
         a = [fp4.quantize(t, fmt=fmt) for t in rand(m, k)]
-        b = [fp4.quantize(t, fmt=fmt) for t in rand(n, k, scale=0.02)]
+        sets = reps if m <= 1024 else 3
+        b = [fp4.quantize(rand(n, k, n=1, scale=0.02)[0], fmt=fmt) for _ in range(sets)]
         v = torch.randn(n, device="cuda") if bias else None
         r = rand(m, n, dtype=dtype)[:1] if residual else [None]
-        return lambda i: fp4.gemm_fused(a[i % 3], b[i % 3], bias=v, act=act, residual=r[0], checkpoint=checkpoint,
+        return lambda i: fp4.gemm_fused(a[i % 3], b[i % sets], bias=v, act=act, residual=r[0], checkpoint=checkpoint,
                                         dtype=dtype)
 
     def norms():
         x, r, g = rand(32768, 4096), rand(32768, 4096), torch.ones(4096, device="cuda")
         o = fp4.rmsnorm(x[0], g, residual=r[0], y=False, y8=True, h8=True, amax=True)
         return (lambda i: fp4.rmsnorm(x[i % 3], g, residual=r[i % 3], y=False, y8=True, h8=True, amax=True),
+                lambda i: fp4.rmsnorm(x[i % 3], g, residual=r[i % 3], h8=True, amax=True),
                 lambda i: fp4.rmsnorm_backward(x[i % 3], o.h8, g, o.rstd, dres=r[i % 3]))
+
+    def one_norm():
+        x, r, g = rand(1, 4096), rand(1, 4096), torch.ones(4096, device="cuda")
+        return (lambda i: fp4.rmsnorm(x[i % 3], g, residual=r[i % 3], amax=True),)
+
+    def norm_gradient(rows, cols, dtype, h8):
+        x, dy, g = rand(rows, cols, dtype=dtype), rand(rows, cols, dtype=dtype), torch.ones(cols, device="cuda")
+        o = fp4.rmsnorm(x[0], g, h8=h8)
+        return (lambda i: fp4.rmsnorm_backward(dy[i % 3], o.h8 if h8 else x[i % 3], g, o.rstd),)
+
+    def small_gradient():
+        dy, z = rand(200, 1001, dtype=f32), rand(200, 1001, dtype=f32)
+        return (lambda i: fp4.act_backward(dy[i % 3], z[i % 3], fp4.FP4_ACT_SILU, amax=True),)
+
+    def small_load():
+        q = [fp4.mx8_quantize(t) for t in rand(1000, 2504, dtype=f32)]
+        return (lambda i: fp4.mx8_dequantize(q[i % 3], f32),)
 
     def gradient():
         dy = rand(4096, 11008)
@@ -111,12 +140,16 @@ def layer(reps: int = LAYER_REPS) -> None:
     nv, mx, none, gelu, silu = fp4.FP4_NVFP4, fp4.FP4_MXFP4, fp4.FP4_ACT_NONE, fp4.FP4_ACT_GELU, fp4.FP4_ACT_SILU
     makers = [norms, gradient, checkpoints,
               lambda: (product(nv, 32768, 11008, 4096, True, gelu, False, True, bf),),
-              lambda: (product(mx, 4096, 4096, 11008, True, none, True, False, torch.float32),),
-              lambda: (product(nv, 512, 4096, 4096, True, silu, False, False, bf),),
+              lambda: (product(mx, 4096, 4096, 11008, True, none, True, False, f32),),
+              *(lambda m=m: (product(nv, m, 4096, 4096, True, silu, False, False, bf),) for m in (128, 512, 1024)),
               lambda: (product(nv, 1, 11008, 4096, True, silu, False, False, bf),),
-              lambda: (product(mx, 24, 4096, 11008, False, none, True, False, bf),)]
+              lambda: (product(mx, 24, 4096, 11008, False, none, True, False, bf),),
+              one_norm, lambda: norm_gradient(333, 1003, f32, False), small_gradient, small_load,
+              lambda: norm_gradient(8192, 11008, f32, False), lambda: norm_gradient(4096, 16384, f32, False),
+              lambda: norm_gradient(4096, 16384, bf, True)]
     for make in makers:
         for call in make():
+            torch.zeros(1 << 30, dtype=torch.uint8, device="cuda")   # what the caches held is gone
             torch.cuda.synchronize()
             marker = torch.zeros(1, device="cuda", dtype=torch.float64)   # one launch of torch's before each operator
             marker.fill_(1.0)
@@ -139,7 +172,8 @@ def summarize_layer(out_dir: str, profiles_dir: str) -> None:
     lines = ["# Kernel time of the operators around the product", "",
              "Command (from the repository root on one MI355X, after `cd /tmp && export TMPDIR=/tmp`; `OUT` = the folder "
              "the run writes its CSV files to):", "", "```", LAYER_COMMAND, "```", "",
-             f"Each operator {LAYER_REPS} times over three sets of inputs in turn; the main launch alone (not the sums' "
+             f"Each operator {LAYER_REPS} times over three sets of inputs in turn (products of up to 1024 rows: over "
+             f"{LAYER_REPS} weight matrices); the main launch alone (not the sums' "
              "reduction or the clearing of a scalar). `TB/s` counts what the operator cannot do without: each input "
              "read once, each output written once.", "",
              "| operator | kernel | median us | min us | TB/s | TFLOP/s |", "|---|---|---|---|---|---|"]
