@@ -164,7 +164,8 @@ constexpr int kEpiFloats = 32 * (32 * FNW + 4) + 32 * 32 * FNW;
 // latency: the residual of the next two sets of 32 rows is on its way in registers
 // (as it lies in memory) while one set is worked on; it goes to LDS so that the loop
 // over the set's rows need not be unrolled (unrolled whole, the accumulators ended
-// in scratch memory).
+// in scratch memory; as it is, 20 B a lane are there in the MXFP4 kernel with bf16
+// outputs, none in the others).
 template <bool OBF, int FNW, bool EDGE>
 __device__ __forceinline__ void epilogue_rows(const EpiArgs& e, float alpha, const v16f (&acc)[FM][FNW], float* stage,
                                               int lane, uint32_t row0, uint32_t col0, uint32_t M, uint32_t N,

@@ -222,10 +222,15 @@ void launch(const GemmArgs& g, const EpiOf<true>& e, hipStream_t s) {
 
 // What a product takes on a shape of this kernel, in us: a start, and for every 256
 // workgroups (one to a CU) a part that does not and a part that does grow with K.
-// Fitted to a sweep of M = 1 .. 2048 by 4096 x 4096, 11008 x 4096, 4096 x 11008 and
-// 1000 x 1280 (N x K), which it follows within about 20%. NVFP4 x 4096 x 4096,
-// measured on the shapes in order: 64 rows 10.0, 9.4, 8.5, 10.2 and 13.3 us; 512
-// rows 51, 42, 33, 30 and 28.6.
+// Fitted to a sweep made before every shape loaded one step ahead; the kernel now
+// takes 0.63 to 1.5 of these times, and the order between the shapes, which is what
+// they are for, mostly stands. Over M = 1 .. 2048 by 4096 x 4096, 11008 x 4096, 4096 x
+// 11008, 2560 x 8192, 1000 x 1280, 2048 x 640 and 8192 x 640 (N x K), both formats,
+// what is picked is within 10% of the best shape (or the tiled kernel) in 138 of 168
+// and 2% slower in the median; the worst are at K = 640 (fp4i_gemm_rows_pays) and
+// 1000 x 1280 (2048 rows NVFP4 18.4 us on 64 x 64, 13.2 on 64 x 32). NVFP4 x 4096 x
+// 4096 on the shapes in order, replays of a graph over three weight matrices: 64 rows
+// 10.4, 9.2, 8.0, 10.2 and 13.8 us; 512 rows 55, 41, 31, 28 and 28.
 struct Shape {
   int mt, nt;
   double nv, mx;   // us per 256 workgroups at K = 4096
@@ -263,8 +268,11 @@ void pick_shape(const GemmArgs& g, const EpiOf<true>& e, hipStream_t s) {
 // Whether the product takes this kernel: the tiled one's time is that of its K
 // tiles (256 values: 4.7 us NVFP4, 1.45 MXFP4, whatever the number of tiles up to
 // one to a CU) after a start and an epilogue of 8 and 7 us. NVFP4 x 4096 x 4096 (N x
-// K), this kernel against that: 64 rows 8.5 us and 44, 512 29 and 48, 1024 47 and
-// 78, 2048 98 and 83; MXFP4 128 rows 8.4 and 24, 512 19 and 26, 1024 28.6 and 29.4.
+// K), this kernel against that with the same epilogue, measured as above: 64 rows 8.2
+// us and 45, 512 28 and 47, 1024 47 and 75, 1536 67 and 76, 2048 94 and 76; MXFP4 128
+// rows 7.6 and 25, 512 19 and 26, 1024 27.7 and 28.8, 1536 40 and 30. Too low for the
+// tiled kernel where K is no multiple of 256 (its K tile is then 128): MXFP4 512 x 8192
+// x 640 takes 18.4 us there, 9.8 on 64 x 32; 2048 x 2048 x 640 18.2 and 9.9.
 bool fp4i_gemm_rows_pays(int64_t M, int64_t N, int64_t K, int fmt) {
   const bool nv = fmt == NV;
   const TilePlan p = fp4i_gemm_tiles(M, N, K);
