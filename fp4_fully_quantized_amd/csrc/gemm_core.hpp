@@ -1125,32 +1125,35 @@ void launch(const GemmArgs& g, const EpiOf<EPI>& epi, hipStream_t s) {
   const uint32_t vec_ok = (g.ldc * es) % 16 == 0 && reinterpret_cast<uintptr_t>(g.c) % 16 == 0;
   float* part = p.ntail ? g.split_ws : nullptr;
   const dim3 grid((p.nfull + NXCD - 1) / NXCD * NXCD);
-  if (p.nfull && FMT == MX && BK == 256) {
+  if (p.nfull) {
+    // One of two kernels by format and K tile; the other is not built for them.
+    if constexpr (FMT == MX && BK == 256) {
 #define FP4_MX8(KERNEL, ...)                                                                                          \
   hipLaunchKernelGGL(KERNEL, grid, dim3(512), 0, s, g.a_codes, g.a_scales, g.b_codes, g.b_scales, (uint32_t)g.M,      \
                      (uint32_t)g.N, (uint32_t)g.K, p.tiles_m, p.tiles_n, group_m, p.nfull, g.c, g.ldc,                 \
                      vec_ok __VA_OPT__(, ) __VA_ARGS__)
-    if constexpr (EPI) {
-      if (g.bf16out) FP4_MX8((k_gemm_mx8_epi<true>), epi);
-      else FP4_MX8((k_gemm_mx8_epi<false>), epi);
-    } else {
-      if (g.bf16out) FP4_MX8((k_gemm_mx8<true>));
-      else FP4_MX8((k_gemm_mx8<false>));
-    }
+      if constexpr (EPI) {
+        if (g.bf16out) FP4_MX8((k_gemm_mx8_epi<true>), epi);
+        else FP4_MX8((k_gemm_mx8_epi<false>), epi);
+      } else {
+        if (g.bf16out) FP4_MX8((k_gemm_mx8<true>));
+        else FP4_MX8((k_gemm_mx8<false>));
+      }
 #undef FP4_MX8
-  } else if (p.nfull) {
+    } else {
 #define FP4_TILES(KERNEL, ...)                                                                                         \
   hipLaunchKernelGGL(KERNEL, grid, block, 0, s, g.a_codes, g.a_scales, g.b_codes, g.b_scales, g.a_tscale, g.b_tscale,  \
                      (uint32_t)g.M, (uint32_t)g.N, (uint32_t)g.K, p.tiles_m, p.tiles_n, group_m, p.nfull, p.ntail,     \
                      p.split, part, g.c, g.ldc, vec_ok __VA_OPT__(, ) __VA_ARGS__)
-    if constexpr (EPI) {
-      if (g.bf16out) FP4_TILES((k_gemm_epi<FMT, BK, true>), epi);
-      else FP4_TILES((k_gemm_epi<FMT, BK, false>), epi);
-    } else {
-      if (g.bf16out) FP4_TILES((k_gemm<FMT, BK, true, false>));
-      else FP4_TILES((k_gemm<FMT, BK, false, false>));
-    }
+      if constexpr (EPI) {
+        if (g.bf16out) FP4_TILES((k_gemm_epi<FMT, BK, true>), epi);
+        else FP4_TILES((k_gemm_epi<FMT, BK, false>), epi);
+      } else {
+        if (g.bf16out) FP4_TILES((k_gemm<FMT, BK, true, false>));
+        else FP4_TILES((k_gemm<FMT, BK, false, false>));
+      }
 #undef FP4_TILES
+    }
   }
   if (p.ntail) {
     // The split pieces after the whole tiles (a partial wave of whole tiles
@@ -1169,16 +1172,16 @@ void launch(const GemmArgs& g, const EpiOf<EPI>& epi, hipStream_t s) {
     else
       hipLaunchKernelGGL((k_split_reduce_epi<FMT, false>), rgrid, block, 0, s, part, p.nfull, p.split, p.tiles_m,
                          p.tiles_n, group_m, g.a_tscale, g.b_tscale, (uint32_t)g.M, (uint32_t)g.N, g.ldc, epi);
-    return;
+  } else {
+    if (g.bf16out)
+      hipLaunchKernelGGL((k_split_reduce<FMT, true>), rgrid, block, 0, s, part, p.nfull, p.split, p.tiles_m,
+                         p.tiles_n, group_m, g.a_tscale, g.b_tscale, (uint32_t)g.M, (uint32_t)g.N, g.c, g.ldc,
+                         vec_ok);
+    else
+      hipLaunchKernelGGL((k_split_reduce<FMT, false>), rgrid, block, 0, s, part, p.nfull, p.split, p.tiles_m,
+                         p.tiles_n, group_m, g.a_tscale, g.b_tscale, (uint32_t)g.M, (uint32_t)g.N, g.c, g.ldc,
+                         vec_ok);
   }
-  if (g.bf16out)
-    hipLaunchKernelGGL((k_split_reduce<FMT, true>), rgrid, block, 0, s, part, p.nfull, p.split, p.tiles_m,
-                       p.tiles_n, group_m, g.a_tscale, g.b_tscale, (uint32_t)g.M, (uint32_t)g.N, g.c, g.ldc,
-                       vec_ok);
-  else
-    hipLaunchKernelGGL((k_split_reduce<FMT, false>), rgrid, block, 0, s, part, p.nfull, p.split, p.tiles_m,
-                       p.tiles_n, group_m, g.a_tscale, g.b_tscale, (uint32_t)g.M, (uint32_t)g.N, g.c, g.ldc,
-                       vec_ok);
 }
 
 // The kernel of a product: its format, and the K tile its K allows.

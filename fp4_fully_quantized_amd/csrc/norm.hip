@@ -486,8 +486,8 @@ struct BwdShape {
 // 768 lanes leave a bf16 row registers for two chunks and gamma (8192 x 11008 bf16 129
 // us; 1024 lanes, whose 128 registers push gamma into LDS, 148). What does not fit all
 // the same goes to scratch memory: fp32 rows 20 B a lane of 768 with h in 8 bits and 68
-// with h as a matrix (8192 x 11008 259 us, 4.2 TB/s), 184 and 216 B of 1024 (4096 x
-// 16384 345 us, 2.3 TB/s); bf16 rows 36 and 24 B of 1024 (4096 x 16384 from 8 bits 88.5
+// with h as a matrix (8192 x 11008 263 us, 4.1 TB/s), 184 and 216 B of 1024 (4096 x
+// 16384 343 us, 2.4 TB/s); bf16 rows 36 and 24 B of 1024 (4096 x 16384 from 8 bits 90
 // us, 3.8 TB/s).
 BwdShape bwd_shape(int64_t rows, int64_t cols) {
   BwdShape b;
