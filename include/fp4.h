@@ -604,8 +604,10 @@ typedef enum fp4_act { FP4_ACT_NONE = 0, FP4_ACT_RELU = 1, FP4_ACT_GELU = 2, FP4
  * does with its fp4_gemm_splitk_bytes more. Products of few tiles (the tokens of
  * a serving loop, small batches, narrow layers; by their sizes alone) run on a
  * kernel of their own that splits K over the waves of a workgroup and takes no
- * workspace beyond RAW operands. C and residual need element alignment only. Also FP4_ERR_NULL for a NULL epi,
- * FP4_ERR_ARG for its enums, FP4_ERR_SHAPE / FP4_ERR_ALIGN for its matrices. */
+ * workspace beyond RAW operands; fp4_gemm has no such kernel, so such a product is
+ * faster here also with nothing in its epilogue. C and residual need element
+ * alignment only. Also FP4_ERR_NULL for a NULL epi, FP4_ERR_ARG for its enums,
+ * FP4_ERR_SHAPE / FP4_ERR_ALIGN for its matrices. */
 typedef struct fp4_epilogue {
     const void* bias;
     const void* residual;
