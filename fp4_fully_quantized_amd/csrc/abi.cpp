@@ -251,13 +251,15 @@ fp4_status check_gemm_pair(const fp4_tensor* A, const fp4_tensor* B, fp4_dtype o
 }
 
 // Every check of a product's epilogue (its matrices are M x N, any alignment
-// of their elements).
-fp4_status check_epilogue(const fp4_epilogue* e, int64_t M, int64_t N) {
+// of their elements; C, checked before, may be the residual as it lies).
+fp4_status check_epilogue(const fp4_epilogue* e, int64_t M, int64_t N, fp4_dtype out_t, const void* C, int64_t ldc) {
   if ((e->bias && !valid_dtype(e->bias_t)) || (e->residual && !valid_dtype(e->residual_t)) || !fp4chk::act_ok(e->act))
     return FP4_ERR_ARG;
   fp4_status st = fp4chk::check_opt(e->bias, e->bias_t, 1, N, N);
   if (st == FP4_OK) st = fp4chk::check_opt(e->residual, e->residual_t, M, N, e->ld_residual);
   if (st == FP4_OK && e->z8) st = fp4chk::check_mx8(e->z8, M, N);
+  if (st == FP4_OK) st = fp4chk::check_over(C, ldc, e->residual, e->ld_residual, M);
+  if (st == FP4_OK && C == e->residual && e->residual_t != out_t) st = FP4_ERR_UNSUPPORTED;
   return st;
 }
 
@@ -400,7 +402,7 @@ fp4_status gemm_impl(const fp4_operand* A, const fp4_operand* B, const fp4_epilo
     if (vb.raw && (st = check_raw(B, vb)) != FP4_OK) return st;
   }
   st = check_gemm_pair(&va.q, &vb.q, out_t, C, ldc);
-  if (st == FP4_OK && epi) st = check_epilogue(epi, va.rows, vb.rows);
+  if (st == FP4_OK && epi) st = check_epilogue(epi, va.rows, vb.rows, out_t, C, ldc);
   if (st != FP4_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   for (int i = 0; i < 2; ++i) {

@@ -58,6 +58,10 @@ fp4_status fp4_rmsnorm(const fp4_rmsnorm_fwd* n, fp4_stream_t stream) {
   if (st == FP4_OK && n->y8) st = check_mx8(n->y8, R, C);
   if (st == FP4_OK && n->h8) st = check_mx8(n->h8, R, C);
   if (st == FP4_OK && (!aligned(n->rstd, 4) || !aligned(n->amax, 4))) st = FP4_ERR_ALIGN;
+  if (st == FP4_OK) st = check_over(n->h, n->ld_h, n->x, n->ld_x, R);
+  if (st == FP4_OK) st = check_over(n->h, n->ld_h, n->residual, n->ld_residual, R);
+  if (st == FP4_OK) st = check_over(n->y, n->ld_y, n->x, n->ld_x, R);
+  if (st == FP4_OK) st = check_over(n->y, n->ld_y, n->residual, n->ld_residual, R);
   if (st != FP4_OK) return st;
   fp4i_launch_rmsnorm(*n, reinterpret_cast<hipStream_t>(stream));
   return launched();
@@ -81,6 +85,8 @@ fp4_status fp4_rmsnorm_backward(const fp4_rmsnorm_bwd* n, fp4_stream_t stream) {
   if (st == FP4_OK && n->h8) st = check_mx8(n->h8, R, C);
   if (st == FP4_OK && (!aligned(n->rstd, 4) || !aligned(n->dgamma, 4))) st = FP4_ERR_ALIGN;
   if (st == FP4_OK && n->dgamma) st = check_ws(n->ws, n->ws_bytes, fp4_rmsnorm_backward_workspace_bytes(R, C));
+  if (st == FP4_OK) st = check_over(n->dx, n->ld_dx, n->dy, n->ld_dy, R);
+  if (st == FP4_OK) st = check_over(n->dx, n->ld_dx, n->dres, n->ld_dres, R);
   if (st != FP4_OK) return st;
   fp4i_launch_rmsnorm_bwd(*n, reinterpret_cast<hipStream_t>(stream));
   return launched();
@@ -102,6 +108,7 @@ fp4_status fp4_act_backward(const fp4_act_bwd* n, fp4_stream_t stream) {
   if (st == FP4_OK && n->z8) st = check_mx8(n->z8, R, C);
   if (st == FP4_OK && (!aligned(n->dbias, 4) || !aligned(n->amax, 4))) st = FP4_ERR_ALIGN;
   if (st == FP4_OK && (n->dbias || n->amax)) st = check_ws(n->ws, n->ws_bytes, fp4_act_backward_workspace_bytes(R, C));
+  if (st == FP4_OK) st = check_over(n->dz, n->ld_dz, n->dy, n->ld_dy, R);
   if (st != FP4_OK) return st;
   fp4i_launch_act_bwd(*n, reinterpret_cast<hipStream_t>(stream));
   return launched();

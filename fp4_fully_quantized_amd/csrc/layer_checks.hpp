@@ -28,6 +28,12 @@ inline fp4_status check_opt(const void* p, int dt, int64_t rows, int64_t cols, i
   return p ? check_mat(p, dt, rows, cols, ld) : FP4_OK;
 }
 
+// An output over an input has its rows where the input's are: others would be
+// written before they are read.
+inline fp4_status check_over(const void* out, int64_t ld_out, const void* in, int64_t ld_in, int64_t rows) {
+  return out && out == in && ld_out != ld_in && rows > 1 ? FP4_ERR_UNSUPPORTED : FP4_OK;
+}
+
 inline fp4_status check_mx8(const fp4_mx8* q, int64_t rows, int64_t cols) {
   if (!q->codes || !q->scales) return FP4_ERR_NULL;
   if (!dims_ok(rows, cols) || q->rows != rows || q->cols != cols) return FP4_ERR_SHAPE;

@@ -523,7 +523,7 @@ fp4_status fp4_mx8_dequantize(const fp4_mx8* q, fp4_dtype dst_t, void* dst, int6
  *             out: what fp4_quantize* take with amax_ready = 1 for these values
  *             (without a rotation). Needs y or y8 (FP4_ERR_NULL).
  * At least one of h, y, y8, h8 is given. Outputs may be the inputs' own buffers
- * (h or y = x or residual, with its leading dimension).
+ * (h or y = x or residual, with its leading dimension, else FP4_ERR_UNSUPPORTED).
  * Errors: FP4_ERR_NULL (x, gamma, no output), FP4_ERR_ARG (dtypes; eps negative
  * or not finite), FP4_ERR_SHAPE, FP4_ERR_ALIGN as fp4_mx8_quantize. */
 typedef struct fp4_rmsnorm_fwd {
@@ -556,7 +556,8 @@ fp4_status fp4_rmsnorm(const fp4_rmsnorm_fwd* n, fp4_stream_t stream);
  *   h / h8 exactly one of them: the forward pass's h, or its 8-bit form.
  *   dres   NULL, or the gradient that reaches h by another way (the residual
  *          stream); added.
- *   dx     may be dy's or dres's own buffer, with its leading dimension.
+ *   dx     may be dy's or dres's own buffer, with its leading dimension (else
+ *          FP4_ERR_UNSUPPORTED).
  *   dgamma device, cols FP32 values, or NULL.
  *   ws     device, 256-byte aligned, at least
  *          fp4_rmsnorm_backward_workspace_bytes(rows, cols) bytes; not needed
@@ -595,7 +596,8 @@ typedef enum fp4_act { FP4_ACT_NONE = 0, FP4_ACT_RELU = 1, FP4_ACT_GELU = 2, FP4
  *   C = act(z) + residual
  *   bias      NULL, or device, N values of bias_t.
  *   residual  NULL, or device, M x N of residual_t, leading dimension
- *             ld_residual >= N; may be C itself (same type and ldc).
+ *             ld_residual >= N; may be C itself (same type and ldc, else
+ *             FP4_ERR_UNSUPPORTED).
  *   z8        NULL, or receives z in 8 bits (M x N): the checkpoint
  *             fp4_act_backward reads.
  * Operands, workspace and errors as fp4_gemm: ws of at least
@@ -629,7 +631,8 @@ fp4_status fp4_gemm_fused(const fp4_operand* A, const fp4_operand* B, const fp4_
  * dgrad and wgrad).
  *   dtype   the type of dy, dz and of z where it is a matrix.
  *   z / z8  exactly one of them: the pre-activation, or its 8-bit form.
- *   dz      may be dy's own buffer, with its leading dimension.
+ *   dz      may be dy's own buffer, with its leading dimension (else
+ *           FP4_ERR_UNSUPPORTED).
  *   dbias   device, cols FP32 values, or NULL.
  *   amax    a device FP32 scalar, or NULL: max |dz| over the stored values as
  *           fp4_tensor_amax takes it, NaN left out: what fp4_quantize* take with
