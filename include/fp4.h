@@ -495,7 +495,8 @@ typedef struct fp4_mx8 {
 
 /* The 8-bit form of the rows x cols matrix src (leading dimension ld), and
  * back: an activation checkpoint, 1.03 bytes a value. q->rows and q->cols are
- * the caller's and must be the matrix's.
+ * the caller's and must be the matrix's. One launch's workgroups hold at least
+ * 2^36 values; a matrix that needs more ends in FP4_ERR_HIP.
  * Errors: FP4_ERR_NULL, FP4_ERR_ARG (dtype), FP4_ERR_SHAPE (rows or cols < 1,
  * ld < cols, q's ld or lds too small or ld % 32 != 0), FP4_ERR_ALIGN (src / dst
  * not aligned to its elements, codes not to 16 bytes). */
