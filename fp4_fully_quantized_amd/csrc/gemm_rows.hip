@@ -17,7 +17,9 @@
 // most of its 35,000 cycles. So a wave loads four lanes to a row (64 bytes of codes
 // in one access; the scales of four steps at once), and turns lanes into rows
 // through an LDS area of its own, which needs no barrier: a wave's LDS accesses run
-// in order. NVFP4 is decoded to f16 exactly and MXFP4 runs on the scaled FP4 MFMA,
+// in order, and the compiler keeps that of a fragment's store and load, whose addresses
+// are the same in some lanes (a wave-wide fence between them changed no result and cost
+// up to 10%: NVFP4 128 x 11008 x 4096 23.9 -> 26.5 us). NVFP4 is decoded to f16 exactly and MXFP4 runs on the scaled FP4 MFMA,
 // as in the tiled kernels.
 #include "epilogue.hpp"
 #include "fp4_device.hpp"
