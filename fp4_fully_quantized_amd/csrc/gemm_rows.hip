@@ -19,8 +19,8 @@
 // through an LDS area of its own, which needs no barrier: a wave's LDS accesses run
 // in order, and the compiler keeps that of a fragment's store and load, whose addresses
 // are the same in some lanes (a wave-wide fence between them changed no result and cost
-// up to 10%: NVFP4 128 x 11008 x 4096 23.9 -> 26.5 us). NVFP4 is decoded to f16 exactly and MXFP4 runs on the scaled FP4 MFMA,
-// as in the tiled kernels.
+// up to 10%: NVFP4 128 x 11008 x 4096 23.9 -> 26.5 us). NVFP4 is decoded to f16 exactly
+// and MXFP4 runs on the scaled FP4 MFMA, as in the tiled kernels.
 #include "epilogue.hpp"
 #include "fp4_device.hpp"
 
